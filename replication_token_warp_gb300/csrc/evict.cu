@@ -147,7 +147,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
         newest = __reduce_max_sync(~0u, newest);
         if (lane == 0) atomicMax(&s.newest, newest);
         sync_all();
-        for (int r = 0; r < blocks; ++r) newest = max(newest, peer(r)->newest);
+        // A block may only read the others' shared memory while they are sure to
+        // run: here the barriers below keep them.  A sequence within its budget
+        // meets no more barriers, and needs no newest position.
+        if (evicts)
+            for (int r = 0; r < blocks; ++r) newest = max(newest, peer(r)->newest);
         // (lens_out may be seq_lens: all blocks have read it by now)
         if (rank == 0 && tid == 0) {
             if (given != len && a.invalid_count != nullptr) atomicAdd(a.invalid_count, 1ull);
