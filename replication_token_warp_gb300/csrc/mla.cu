@@ -341,12 +341,19 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
         if (!have) break;
         some = true;
         buffer ^= 1;
-        const int begin = next.begin, end = next.end;
+        // The unit up to which some row may have no reference: it has seen no key
+        // (skipped blocks, or scores of -inf), its sums and accumulators are 0,
+        // and the first unit that shows it one gives it its reference.  Until
+        // then -inf stands as 0.
+        int fresh = next.begin;
+        const int end = next.end;
 
         const int prefix = next.s.len - next.s.count;
 #pragma unroll
         for (int c = 0; c < kC / 2; ++c) l[c] = make_float2(0.f, 0.f);
         ref = -INFINITY;
+        if (t.lane < kC) m.nref[row0 + t.lane] = kShift;
+        __syncwarp();
         texp = 0;
         int par = 0;                    // which of m.grown is in use
         // The next unit's scores are read while this unit's probabilities wait
@@ -364,8 +371,8 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
 #pragma unroll 1
         for (int i = 0; i < S::kBunches; ++i) add(n, i);
 
-        for (int u = begin; u < end; ++u) {
-            const bool first = u == begin;
+        for (int u = fresh; u < end; ++u) {
+            const bool unset = u == fresh;
             const uint4 info = m.keys[t.key];
             const uint32_t tnew = m.ratios;
             __syncwarp();
@@ -378,8 +385,7 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
 #pragma unroll
             for (int c = 0; c < kC / 4; ++c) {
                 const float4 f = *reinterpret_cast<const float4 *>(&m.factor[row0 + 4 * c]);
-                const float4 r = first ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                       : *reinterpret_cast<const float4 *>(&m.nref[row0 + 4 * c]);
+                const float4 r = *reinterpret_cast<const float4 *>(&m.nref[row0 + 4 * c]);
                 z[2 * c] = fma2(z[2 * c], make_float2(f.x, f.y), add2(gexp2, make_float2(r.x, r.y)));
                 z[2 * c + 1] =
                     fma2(z[2 * c + 1], make_float2(f.z, f.w), add2(gexp2, make_float2(r.z, r.w)));
@@ -400,19 +406,20 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
             // Where nothing outgrows its reference one barrier settles that.
             constexpr float kMost = kShift + kGrowth;
             // What did is gathered row by row: few do.
-            if (!first && top > kMost) {
+            if (!unset && top > kMost) {
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
                     const float w = c & 1 ? z[c / 2].y : z[c / 2].x;
                     if (w > kMost) atomicMax(&m.grown[par][row0 + c], __float_as_int(w));
                 }
             }
-            const bool moves = any_of_part(1 + t.part, top > kMost || first || tnew != texp);
+            const bool moves = any_of_part(
+                1 + t.part, top > (unset ? -INFINITY : kMost) || tnew != texp);
             uint32_t rows = 0;      // that moved, a bit each
             if (moves) {
                 const int r = row0 + (t.lane & (kC - 1));
                 float mine = -INFINITY;     // row r's new maximum, where it has one
-                if (first) {
+                if (unset) {
 #pragma unroll
                     for (int c = 0; c < kC; ++c) {
                         const float w = warp_max(c & 1 ? z[c / 2].y : z[c / 2].x);
@@ -432,17 +439,21 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
                     par = par == 2 ? 0 : par + 1;
                 }
                 // back from relative to the reference (-inf stands as 0)
-                const float was = first || ref == -INFINITY ? 0.f : ref;
-                const float now = first ? mine : mine + (was - kShift);
+                const float was = ref == -INFINITY ? 0.f : ref;
+                const float now = mine + (was - kShift);
                 const float old = ref;
                 if (now > ref) ref = now;
+                if (unset) {
+                    if (now != now) ref = 0.f;     // scores of NaN alone: no maximum
+                    if (__any_sync(~0u, ref == -INFINITY)) fresh = u + 1;
+                }
                 rows = __ballot_sync(~0u, t.lane < kC && old != ref);
                 const float moved = ref == -INFINITY ? 0.f : ref;
                 m.nref[r] = kShift - moved;
                 m.fac[r] = old == ref ? 1.f : exp2_approx(old - ref);
                 // z moves by the change of what it is relative to (through
                 // shared memory, which is cheaper than a shuffle a row)
-                m.shift[r] = first ? kShift - moved : was - moved;
+                m.shift[r] = was - moved;
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < kC / 4; ++c) {
@@ -453,6 +464,8 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
                     l[2 * c] = mul2(l[2 * c], make_float2(f.x, f.y));
                     l[2 * c + 1] = mul2(l[2 * c + 1], make_float2(f.z, f.w));
                 }
+            } else if (unset) {
+                fresh = u + 1;
             }
 
             // probabilities, their sum in fp32, and in fp16 for the products
@@ -466,9 +479,9 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
                 l[c] = fma2(x, ginv2, l[c]);
                 p[c] = half2_from(x.x, x.y);
             }
-            if (moves && !first) {
+            if (moves && texp != 0) {
                 // The accumulators follow the references, once the last
-                // unit's values are in.
+                // unit's values are in (without ratios so far there are none).
                 const Ring<S::kProbs> last = probs_at(n - 1, S::kGroups - 1);
                 wait(bars.prob_empty(last.at), last.pass);
                 tcgen05_after_sync();
