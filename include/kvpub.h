@@ -345,7 +345,8 @@ kvpub_status kvpub_epoch_wait(const unsigned long long *epoch,
  *                sequence's length are not read.
  *  seq_lens      int32 [num_seqs]: the cached tokens of each sequence, its
  *                query tokens' own rows among them (publish first).
- *  num_seqs      0..65535. With 0 sequences or tokens the call does nothing.
+ *  num_seqs      0..65535. With 0 sequences the call does nothing; nor does
+ *                attention with 0 tokens, which needs no pointers then.
  *  max_query_len 1..KVPUB_MAX_QUERY_TOKENS: at least the number of query
  *                tokens of any sequence.
  *  query_start   int32 [num_seqs + 1], non-decreasing: the query tokens of
@@ -425,6 +426,9 @@ kvpub_status kvpub_mla_tree_fp8(
  *
  *  lse          the attention call's, for the same queries and keys. A row
  *               whose lse is -inf adds nothing.
+ *  num_tokens   a sequence without query tokens gets decay * weights_in, also
+ *               where no sequence has any (0 tokens: query_start is given,
+ *               and lse, q_latent and q_rope are not used).
  *  query_start  as above, or NULL for one query token a sequence.
  *  weights_in   float [num_seqs, >= width], row stride
  *               weights_in_stride, or NULL for zeros.

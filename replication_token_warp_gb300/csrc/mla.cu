@@ -935,7 +935,7 @@ kvpub_status attention(const MlaCall &c, void *out, int64_t out_token, int64_t o
                        cudaStream_t stream) {
     MlaArgs a;
     bool empty;
-    kvpub_status st = check_call(c, &a, &empty);
+    kvpub_status st = check_call(c, false, &a, &empty);
     if (st != KVPUB_OK) return st;
     if (empty) return ok();
     if (out == nullptr) return fail(KVPUB_ERR_INVALID_ARG, "out is NULL");

@@ -46,8 +46,9 @@ struct MlaCall {
     unsigned long long *invalid_count;
 };
 
-// What the three calls check alike.  *empty: there is nothing to do.
-inline kvpub_status check_call(const MlaCall &c, MlaArgs *out, bool *empty) {
+// What the three calls check alike.  *empty: there is nothing to do.  sums: a
+// sequence without query tokens has a sum to update.
+inline kvpub_status check_call(const MlaCall &c, bool sums, MlaArgs *out, bool *empty) {
     *empty = false;
     if (c.block_size != KVPUB_BLOCK_SIZE)
         return fail(KVPUB_ERR_INVALID_ARG, "block_size %d != %d", c.block_size, KVPUB_BLOCK_SIZE);
@@ -77,14 +78,15 @@ inline kvpub_status check_call(const MlaCall &c, MlaArgs *out, bool *empty) {
         return fail(KVPUB_ERR_INVALID_ARG, "softmax_scale is not a positive finite number");
     if (c.invalid_count != nullptr && !aligned(c.invalid_count, 8))
         return fail(KVPUB_ERR_ALIGNMENT, "invalid_count is not 8-byte aligned");
-    if (c.num_tokens == 0) {
+    if (c.num_seqs == 0 || (c.num_tokens == 0 && !sums)) {
         *empty = true;
         return KVPUB_OK;
     }
     kvpub_status st;
-    if ((st = check_q(c.q_latent, c.q_latent_token, c.q_latent_head, "q_latent")) != KVPUB_OK)
+    if (c.num_tokens > 0 &&
+        ((st = check_q(c.q_latent, c.q_latent_token, c.q_latent_head, "q_latent")) != KVPUB_OK ||
+         (st = check_q(c.q_rope, c.q_rope_token, c.q_rope_head, "q_rope")) != KVPUB_OK))
         return st;
-    if ((st = check_q(c.q_rope, c.q_rope_token, c.q_rope_head, "q_rope")) != KVPUB_OK) return st;
     if (c.main_cache == nullptr) return fail(KVPUB_ERR_INVALID_ARG, "main_cache is NULL");
     if (!aligned(c.main_cache, 16))
         return fail(KVPUB_ERR_ALIGNMENT, "main_cache is not 16-byte aligned");

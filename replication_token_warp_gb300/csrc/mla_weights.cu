@@ -299,13 +299,15 @@ extern "C" kvpub_status kvpub_mla_weights_fp8(
                     softmax_scale, invalid_count};
     MlaArgs a;
     bool empty;
-    kvpub_status st = check_call(c, &a, &empty);
+    kvpub_status st = check_call(c, true, &a, &empty);
     if (st != KVPUB_OK) return st;
     if (!(fabsf(decay) <= 3.402823466e38f))
         return fail(KVPUB_ERR_INVALID_ARG, "decay is not finite");
     if (width < 0) return fail(KVPUB_ERR_INVALID_ARG, "width %lld < 0", (long long)width);
     if (empty || width == 0) return ok();
-    if (lse == nullptr || weights_out == nullptr)
+    // no query tokens, and sums that stay as they are
+    if (num_tokens == 0 && weights_in == weights_out && decay == 1.f) return ok();
+    if ((num_tokens > 0 && lse == nullptr) || weights_out == nullptr)
         return fail(KVPUB_ERR_INVALID_ARG, "lse or weights_out is NULL");
     if (!aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4))
         return fail(KVPUB_ERR_ALIGNMENT, "lse, weights_in or weights_out is misaligned");
