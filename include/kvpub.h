@@ -432,7 +432,8 @@ kvpub_status kvpub_mla_tree_fp8(
  *  query_start  as above, or NULL for one query token a sequence.
  *  weights_in   float [num_seqs, >= width], row stride
  *               weights_in_stride, or NULL for zeros.
- *  weights_out  float, the same shape; may be weights_in (same stride).
+ *  weights_out  float, the same shape; may be weights_in (with the same
+ *               stride, where there is more than one row).
  *  decay        finite.
  */
 kvpub_status kvpub_mla_weights_fp8(
@@ -473,8 +474,8 @@ size_t kvpub_evict_workspace_bytes(int64_t num_seqs, int64_t budget);
  *  weights_out, positions_out
  *                 [num_seqs, >= min(budget, width)]: the entries of the
  *                 tokens that stay, by their new place. Each may be its
- *                 input (with the same stride). positions_out may be NULL
- *                 if positions_in is.
+ *                 input (with the same stride, where there is more than one
+ *                 row). positions_out may be NULL if positions_in is.
  *  lens_out       int32 [num_seqs]: min(length, budget). May be seq_lens.
  *  main_caches, indexer_caches, num_replicas, num_blocks, block_size
  *                 as in kvpub_store_mla_fp8. No two sequences may share a

@@ -529,9 +529,10 @@ extern "C" kvpub_status kvpub_evict_fp8(
         !aligned(block_table, 4) || !aligned(weights_out, 4) || !aligned(positions_out, 4) ||
         !aligned(lens_out, 4))
         return fail(KVPUB_ERR_ALIGNMENT, "a weights, positions, length or table pointer is misaligned");
-    if ((weights_in == weights_out && weights_in_stride != weights_out_stride) ||
-        (positions_in != nullptr && positions_in == positions_out &&
-         positions_in_stride != positions_out_stride))
+    // (a single row has no use for its stride)
+    if (num_seqs > 1 && ((weights_in == weights_out && weights_in_stride != weights_out_stride) ||
+                         (positions_in != nullptr && positions_in == positions_out &&
+                          positions_in_stride != positions_out_stride)))
         return fail(KVPUB_ERR_INVALID_ARG, "in place needs one row stride");
     const size_t bytes = kvpub_evict_workspace_bytes(num_seqs, budget);
     if (workspace == nullptr) return fail(KVPUB_ERR_WORKSPACE, "workspace is NULL");

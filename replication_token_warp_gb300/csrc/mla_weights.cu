@@ -316,7 +316,8 @@ extern "C" kvpub_status kvpub_mla_weights_fp8(
         (weights_in != nullptr && (weights_in_stride < width || weights_in_stride > most)))
         return fail(KVPUB_ERR_INVALID_ARG, "weights row stride below width %lld",
                     (long long)width);
-    if (weights_in == weights_out && weights_in_stride != weights_out_stride)
+    // (a single row has no use for its stride)
+    if (num_seqs > 1 && weights_in == weights_out && weights_in_stride != weights_out_stride)
         return fail(KVPUB_ERR_INVALID_ARG, "weights in place need one row stride");
     a.lse_in = lse;
     a.weights_in = weights_in;

@@ -1,4 +1,4 @@
-"""The weights call where no sequence has query tokens."""
+"""Further uses of the weights call: no query tokens, one sequence in place."""
 
 import numpy as np
 import pytest
@@ -50,3 +50,16 @@ def test_sums_decay_without_query_tokens(dev, heads, longest):
     kvpub.mla_weights_fp8(p.ql[:1], p.qr[:1], p.lse[:1], p.d_cache, p.d_table, p.d_lens, base.SCALE, w, mixed, 0.75, start, None,
                           longest, p.num_blocks)
     assert torch.equal(mixed[1:], out[1:])
+
+
+@pytest.mark.parametrize("batch", [1, 2])
+def test_in_place_in_a_narrower_view(dev, batch):
+    """The sums' first columns as the output: one row's stride does not matter."""
+    p = base.Problem([300] * batch, 16, seed=3).on(dev)
+    p.run()
+    w = torch.rand(batch, 400, device=dev)
+    want = torch.empty(batch, 250, device=dev)
+    base.weights_call(p, p.lse, w, want, 0.5)
+    same = w.clone()
+    base.weights_call(p, p.lse, same, same[:, :250], 0.5)
+    assert torch.equal(same[:, :250], want) and torch.equal(same[:, 250:], w[:, 250:])
