@@ -864,7 +864,14 @@ struct Split {
     int cluster;      // blocks an item, 0: cut by find_work and joined by a second launch
 };
 
-Split split_work(const MlaCall &c, int sms, const int (&clusters)[3]) {
+template <int kRows>
+kvpub_status attention_clusters(int dev, int (*out)[3]) {
+    using S = Shape<kRows, true>;
+    return clusters_at_once<mla_attention_kernel<kRows, true>>(dev, S::kThreads, smem_bytes<S>(),
+                                                               out);
+}
+
+Split split_work(const MlaCall &c, int sms, const int (&clusters)[3][3]) {
     const int most = rows_for(c.num_heads, c.max_query_len);
     const int64_t units = units_at_most(c.max_blocks);
     const int64_t unit_cost[3] = {42, 51, 80}, segment_cost[3] = {90,140,170};
@@ -883,7 +890,7 @@ Split split_work(const MlaCall &c, int sms, const int (&clusters)[3]) {
         }
         for (int j = 0; j <= 3 && 1 << j < 2 * units; ++j) {
             const int k = 1 << j;
-            if (items > (j == 0 ? sms : clusters[j - 1])) break;     // all at once
+            if (items > (j == 0 ? sms : clusters[i][j - 1])) break;     // all at once
             const int64_t each = segment_cost[i] + (units + k - 1) / k * unit_cost[i] +
                                  (j == 0 ? 0 : cluster_cost[i]);
             if (each < best) {
@@ -969,9 +976,10 @@ kvpub_status attention(const MlaCall &c, void *out, int64_t out_token, int64_t o
     if ((st = map_cache(a, 128, CU_TENSOR_MAP_SWIZZLE_128B, &tiles)) != KVPUB_OK ||
         (st = map_cache(a, 16, CU_TENSOR_MAP_SWIZZLE_NONE, &scales)) != KVPUB_OK)
         return st;
-    int clusters[3];
-    if ((st = clusters_at_once(dev, mla_attention_kernel<16, true>, Shape<16, true>::kThreads,
-                               smem_bytes<Shape<16, true>>(), &clusters)) != KVPUB_OK)
+    int clusters[3][3];     // with 16, 32 and 64 rows
+    if ((st = attention_clusters<16>(dev, &clusters[0])) != KVPUB_OK ||
+        (st = attention_clusters<32>(dev, &clusters[1])) != KVPUB_OK ||
+        (st = attention_clusters<64>(dev, &clusters[2])) != KVPUB_OK)
         return st;
     const Split split = split_work(c, sms < kMaxCtas ? sms : kMaxCtas, clusters);
     Workspace ws;

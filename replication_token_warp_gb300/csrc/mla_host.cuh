@@ -147,11 +147,11 @@ kvpub_status launch_opted(const char *name, void (*kernel)(KArgs...), std::atomi
     }
 }
 
-// How many clusters of 2, 4 or 8 blocks fit the GPU at once, of a kernel whose
-// blocks take an SM each (152 SMs hold 76, 36 and 15), asked for once a device.
-template <typename... KArgs>
-kvpub_status clusters_at_once(int dev, void (*kernel)(KArgs...), int threads, int bytes,
-                              int (*out)[3]) {
+// How many clusters of 2, 4 or 8 blocks of a kernel fit the GPU at once (of blocks
+// that take an SM each, 152 SMs hold 76, 36 and 15), asked for once a device.  `Kernel`
+// is an argument of the template so that each kernel has its own answers.
+template <auto Kernel>
+kvpub_status clusters_at_once(int dev, int threads, int bytes, int (*out)[3]) {
     static std::atomic<int> cached[kMaxDevices][3];
     for (int i = 0; i < 3; ++i) {
         int n = cached[dev][i].load(std::memory_order_relaxed);
@@ -168,8 +168,8 @@ kvpub_status clusters_at_once(int dev, void (*kernel)(KArgs...), int threads, in
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             cudaError_t e = cudaFuncSetAttribute(
-                (const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+                (const void *)Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg);
             if (e != cudaSuccess)
                 return fail(KVPUB_ERR_CUDA, "clusters: %s", cudaGetErrorString(e));
             cached[dev][i].store(n, std::memory_order_relaxed);

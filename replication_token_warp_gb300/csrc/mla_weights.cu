@@ -263,8 +263,8 @@ kvpub_status launch_weights(const MlaArgs &a, const CUtensorMap &tiles, const CU
         int dev, clusters[3];
         kvpub_status st = current_device(&dev);
         if (st == KVPUB_OK)
-            st = clusters_at_once(dev, mla_weights_kernel<64, true>, S::kThreads, smem_bytes<S>(),
-                                  &clusters);
+            st = clusters_at_once<mla_weights_kernel<64, true>>(dev, S::kThreads, smem_bytes<S>(),
+                                                                &clusters);
         if (st != KVPUB_OK) return st;
         const int64_t units = static_cast<int64_t>(a.num_seqs) * units_at_most(a.max_blocks);
         const int tiles_most = (a.num_heads * a.max_query_len + S::kRows - 1) / S::kRows;
