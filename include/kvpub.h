@@ -361,9 +361,9 @@ kvpub_status kvpub_epoch_wait(const unsigned long long *epoch,
  *                seen. The call adds the number of skipped blocks to the
  *                counter, one for every sequence whose length is negative
  *                or above max_blocks * 64 (the length is clamped), and one
- *                for every wait inside a kernel that ran into its limit
- *                (which no correct launch does; the outputs of that call
- *                are then not to be used).
+ *                for every block of threads in which a wait ran into its
+ *                limit (which no correct launch does). What such a block
+ *                writes afterwards is NaN, with or without a counter.
  *  lse           float [num_tokens, num_heads], contiguous.
  * Nothing else is read: rows of the cache past a sequence's length may hold
  * anything, also NaN codes, and a NaN or Inf in a row reaches only the query

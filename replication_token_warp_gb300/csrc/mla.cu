@@ -222,8 +222,6 @@ __device__ __forceinline__ float column_sums(const float2 (&l)[kC / 2], int lane
     return v[0];
 }
 
-// After a wait that ran into its limit the role goes on without waiting: its
-// named barriers need all of its warps.
 template <class S, bool kCluster>
 __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *smem,
                              Misc<S> &m, Segments<S> source, int blocks) {
@@ -260,6 +258,7 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
             if (t.lane < kC) {
                 const int r = row0 + t.lane;
                 total = ((m.wmax[0][r] + m.wmax[1][r]) + m.wmax[2][r]) + m.wmax[3][r];
+                if (m.abort != 0) total = NAN;      // see Waiter
                 const float lse2 = total == 0.f ? -INFINITY
                                                 : (ref == -INFINITY ? 0.f : ref) - kShift +
                                                       log2f(total);
@@ -303,7 +302,7 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
                 float o[kC];
                 tmem_load<kC>(t.tmem + i * S::kRows + row0, o);
                 tmem_load_wait();
-                const float up = byte_ratio(texp, i);
+                const float up = wait.alive ? byte_ratio(texp, i) : NAN;
                 const int dim = i * 128 + t.key;
 #pragma unroll
                 for (int c = 0; c < kC; ++c) o[c] *= m.fac[row0 + c] * up;

@@ -160,7 +160,9 @@ struct Bars {
 };
 
 // Waits of a role whose warps must not leave it (it has named barriers to
-// keep): after one that ran out it goes on without waiting.
+// keep): after one that ran out it goes on without waiting, and what it writes
+// then is NaN.  Where another role gave up, these waits run out too: they are
+// for what that role no longer hands on.
 template <class S>
 struct Waiter {
     Misc<S> &m;

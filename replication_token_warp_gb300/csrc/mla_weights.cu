@@ -171,7 +171,7 @@ __device__ void sum_role(const MlaArgs &a, uint8_t *smem, Misc<S> &m, Source sou
                 }
                 sum2 = add2(sum2, add2(x, y));
             }
-            float sum = on ? sum2.x + sum2.y : 0.f;
+            float sum = !wait.alive ? NAN : on ? sum2.x + sum2.y : 0.f;     // see Waiter
             // two buffers: a part is at most one barrier ahead
             float *part = sums + (u & 1) * 3 * kUnit;
             if (t.part > 0) part[(t.part - 1) * kUnit + t.key] = sum;
