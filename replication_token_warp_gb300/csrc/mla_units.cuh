@@ -417,7 +417,8 @@ __device__ void load_role(const MlaArgs &a, const CUtensorMap *tiles, const CUte
 
 // Softmax warps: the segment's query rows into shared memory, each scaled by
 // a power of two to a largest value in [128, 256) and split into E4M3 and
-// E5M2 (exact for values above 2^-14 of the largest), the rope kept in bf16.
+// E5M2 (exact for values of at least 2^-13 of the largest, the others off by at
+// most 2^-21 of it), the rope kept in bf16.
 template <class S>
 __device__ void load_queries(const MlaArgs &a, const Segment &g, uint8_t *smem, Misc<S> &m,
                              int64_t *out_at) {
