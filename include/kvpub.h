@@ -330,6 +330,16 @@ kvpub_status kvpub_epoch_wait(const unsigned long long *epoch,
  * over the keys k that t sees. A row that sees no key gets out 0 and lse
  * -inf. The value up-projection is the caller's matrix product.
  *
+ * Accuracy. Scores, maxima, sums and accumulators are fp32. A query value
+ * below 2^-13 of its row's largest is held to 2^-21 of that largest, the
+ * others exactly. Probabilities multiply the values in 8 significant bits, as
+ * bf16 has, as long as they are not tiny: of a value's tile of 128, the
+ * smallest step is 2^-20 of the row's largest (probability times the key's
+ * largest tile scale), times the tile's largest ratio of a key's scale to
+ * that key's largest. So where one key alone has a tile whose scale is some
+ * 2^14 or more above its other tiles' scales, few bits are left in those
+ * other tiles. lse and the weights are formed from fp32 probabilities.
+ *
  * Arguments that the three calls share:
  *  q_latent      bf16 [num_tokens, num_heads, >= 512]; q_rope bf16
  *                [num_tokens, num_heads, >= 64]. Token and head strides are
@@ -342,7 +352,11 @@ kvpub_status kvpub_epoch_wait(const unsigned long long *epoch,
  *  block_table   int32 [num_seqs, >= max_blocks], row stride
  *                block_table_stride elements. Key k of sequence b is in slot
  *                block_table[b, k / 64] * 64 + k % 64. Entries past a
- *                sequence's length are not read.
+ *                sequence's length are not read. How a call is cut (rows of a
+ *                tile, blocks, clusters) follows max_blocks, as the lengths are
+ *                on the GPU: small calls are fastest with no more columns than
+ *                their longest sequence needs (a tree of 8 drafts over 777
+ *                tokens takes 13.7 us with 13 columns, 21.3 with 640).
  *  seq_lens      int32 [num_seqs]: the cached tokens of each sequence, its
  *                query tokens' own rows among them (publish first).
  *  num_seqs      0..65535. With 0 sequences the call does nothing; nor does
@@ -470,7 +484,9 @@ size_t kvpub_evict_workspace_bytes(int64_t num_seqs, int64_t budget);
  *  positions_in   int32, the same shape and its own stride, or NULL: place
  *                 k holds position k.
  *  width          columns of both, at most 2^30; a sequence longer than width (or than
- *                 max_blocks * 64) is cut to it and counted as invalid.
+ *                 max_blocks * 64) is cut to it and counted as invalid. The
+ *                 smaller of the two decides how the call is cut (1 sequence
+ *                 of 700 tokens: 6.8 us of GPU time, with 40,960 columns 17.6).
  *  weights_out, positions_out
  *                 [num_seqs, >= min(budget, width)]: the entries of the
  *                 tokens that stay, by their new place. Each may be its
@@ -478,8 +494,9 @@ size_t kvpub_evict_workspace_bytes(int64_t num_seqs, int64_t budget);
  *                 row). positions_out may be NULL if positions_in is.
  *  lens_out       int32 [num_seqs]: min(length, budget). May be seq_lens.
  *  main_caches, indexer_caches, num_replicas, num_blocks, block_size
- *                 as in kvpub_store_mla_fp8. No two sequences may share a
- *                 block among their first `budget` places. A row whose source
+ *                 as in kvpub_store_mla_fp8. A block among a sequence's
+ *                 first `budget` places may be in no other sequence, unless
+ *                 neither is longer than the budget. A row whose source
  *                 or destination block is not in [0, num_blocks) is not
  *                 moved, and is counted in invalid_count.
  *  workspace      kvpub_evict_workspace_bytes(num_seqs, budget) bytes,

@@ -356,8 +356,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
 // the second), and then the rows follow one another, the loads of kReplicas
 // replicas before their stores.  A row is 41 chunks of 16 bytes in the Main
 // cache, 8 in the Indexer cache, and its scale.  The loads of more rows before
-// their stores cost the registers of the warps that hide them: 2 x 2 rows took
-// 46 us instead of 40 for 64 x 8,192 places in two replicas.
+// their stores cost the registers of the warps that hide them: when this was
+// tried, 2 x 2 rows made 64 sequences of up to 8,192 places in two replicas take
+// 46 us instead of 40.
 template <int kReplicas>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
     wait_previous_kernel();
@@ -578,8 +579,8 @@ extern "C" kvpub_status kvpub_evict_fp8(
         return st;
     // As few moves a warp as leave 32 warps an SM, if all that can move do, and
     // 8 at most: alone a move's latency counts, in a large launch the look-ups
-    // before the rows do (64 x 8,192 places in two replicas: 49 us with 1, 40
-    // with 8, 55 with 16, which leave too few warps).
+    // before the rows do (64 sequences of 513 to 8,192 places in two replicas: 51.5 us
+    // with 1, 44.3 with 8, 59 with 16, which leave too few warps).
     const int64_t most_moves = longest <= budget ? 0 : budget < longest - budget ? budget : longest - budget;
     a.batch = 1;
     while (a.batch < 8 && most_moves * num_seqs > static_cast<int64_t>(sms) * 32 * a.batch)

@@ -40,12 +40,12 @@
 //
 // What bounds it.  With 16 rows the keys' loads: a unit takes some 4,200
 // cycles, where 80 KB of cache take 3,650 at the memory's rate (64 ragged
-// sequences of up to 40k tokens, 16 heads: 51 us, half of the memory's rate
+// sequences of up to 40k tokens, 16 heads: 52 us, half of the memory's rate
 // with what starts, ends and joins).  With 64 rows the softmax warps between
 // the products: a unit takes some 7,700 cycles, its products 3,300 (reading
 // their operands from shared memory), its instructions 3,200 issue slots of
-// each scheduler (48 sequences of 8k tokens, 64 heads: 108 us, 2.4 TB/s; 64
-// drafts of 64 heads over 4 x 16k tokens: 661 us, 0.70 PFLOP/s).
+// each scheduler (48 sequences of 8k tokens, 64 heads: 109 us, 2.4 TB/s; 64
+// drafts of 64 heads over 4 x 16k tokens: 670 us, 0.69 PFLOP/s).
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -290,7 +290,7 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
             if (t.lane == 0) mbar_arrive(bars.query_ready());
         }
         // The join's launch overlaps with the last results: 64 ragged sequences
-        // of 16 heads 74 -> 67 us, at 64 rows no difference.
+        // of 16 heads 52.5 -> 51.8 us, at 64 rows no difference.
         if (!have && !kCluster) launch_next_kernel();
         if (some) {
             __syncwarp();
@@ -485,8 +485,8 @@ __device__ void softmax_role(const MlaArgs &a, const Workspace &ws, uint8_t *sme
                 wait(bars.prob_empty(last.at), last.pass);
                 tcgen05_after_sync();
                 // Mostly a row or two: their columns of the four tiles at once
-                // take 0.2 us a row, all of the thread's 0.8 (a tree of 64 drafts
-                // over 4 x 16k tokens 676 us, without this 704).
+                // take 0.2 us a row, all of the thread's 0.8 (when this was added, a
+                // tree of 64 drafts over 4 x 16k tokens went from 704 to 676 us).
                 if (tnew == texp && __popc(rows) <= 4) {
                     for (; rows != 0; rows &= rows - 1) {
                         const int c = __ffs(rows) - 1;
@@ -767,8 +767,8 @@ template <int kRows>
 __global__ void __launch_bounds__(kJoinDims)
 mla_join_kernel(const MlaArgs a, const Workspace ws) {
     // parts in flight: with 16 rows an item has more parts and the grid fewer
-    // blocks (64 ragged sequences, 16 heads: 50.9 us with 8, 51.7 with 4; 48 of 8k
-    // tokens, 64 heads: 110.2 and 108.5)
+    // blocks (when measured: 64 ragged sequences, 16 heads 50.9 us with 8, 51.7 with 4;
+    // 48 of 8k tokens, 64 heads 110.2 and 108.5)
     constexpr int kJoinParts = kRows == 16 ? 8 : 4;
     wait_previous_kernel();
     const int x = blockIdx.x, lane = threadIdx.x & 31;
@@ -850,14 +850,15 @@ mla_join_kernel(const MlaArgs a, const Workspace ws) {
 // 11,000. Large calls take the most rows that their sequences fill and runs of
 // equal length; smaller ones what gives the shortest run by the longest lengths
 // that the block table allows, and if one cluster (or block) an item does that
-// and all fit the GPU at once, without the second launch. Measured, us:
-//                                             runs with 16, 32, 64 rows; clusters
-//   1 sequence, 16 heads, 509 tokens              11.0                    10.1
-//   1 tree of 8 drafts, 16 heads, 777 tokens      14.6   18    24         13.6
-//   2 sequences, 128 heads, 3,000 tokens          19.8   21.6  24         25 (two rounds)
-//   4 trees of 3 drafts, 32 heads, 5,000 tokens   23.3   23.7  36         26.6
-//   50 sequences, 64 heads, up to 751 tokens      28.8   29.7  34         26.0
-//   42 sequences, 128 heads, up to 78 tokens      26     23    18.9       15.7
+// and all fit the GPU at once, without the second launch. Measured in a graph, us
+// (* is what the rule takes, not always the best: it knows only the longest length):
+//                                                runs with 16, 32, 64 rows   clusters
+//   1 sequence, 16 heads, 509 tokens              10.5                       10.0* (4 blocks, 16 rows)
+//   1 tree of 8 drafts, 16 heads, 777 tokens      13.4   15.7   19.6         13.8* (8 blocks, 16 rows)
+//   2 sequences, 128 heads, 3,000 tokens          21.8*  22.0   23.9         20.8  (4 blocks, 16 rows)
+//   4 trees of up to 3 drafts, 32 heads, 5,000    24.6   28.8*  37.4         41.0  (4 blocks, 32 rows)
+//   50 sequences, 64 heads, 15 to 751 tokens      27.7   25.6*  23.2         35.6  (a block, 64 rows)
+//   42 sequences, 128 heads, 2 to 78 tokens       26.8   23.0   19.2         16.0* (a block, 64 rows)
 struct Split {
     int rows, blocks;
     int cluster;      // blocks an item, 0: cut by find_work and joined by a second launch

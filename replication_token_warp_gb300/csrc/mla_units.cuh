@@ -52,9 +52,9 @@ struct Shape {
     // What a segment costs beside its units, in units (queries in, results
     // out and joined, the pipeline's start, first units that move their
     // references more often). Measured without it and with 1 to 4, us: 24 ragged
-    // trees of 32 heads (64 rows) 124, 103, 94, 92, 96; 28 sequences of 10k
-    // tokens, 32 heads (32 rows) with 2 to 4 64, 65, 66; 64 ragged sequences of 16
-    // heads 67, 60, 55, 56, 57.
+    // trees of 32 heads (64 rows) 115, 99, 81, 80, 84; 28 sequences of 10k
+    // tokens, 32 heads (32 rows) 68, 65, 64, 67, 67; 64 ragged sequences of 16
+    // heads 64, 57, 52, 54, 54.
     static constexpr int kOver = !kValues ? 0 : kRows <= 32 ? 2 : 3;
     static constexpr int kColumns = kRows == 16 ? 256 : 512;   // tensor memory
     static constexpr int kQueryTile = kRows * 128;
