@@ -332,13 +332,14 @@ kvpub_status kvpub_epoch_wait(const unsigned long long *epoch,
  *
  * Accuracy. Scores, maxima, sums and accumulators are fp32. A query value
  * below 2^-13 of its row's largest is held to 2^-21 of that largest, the
- * others exactly. Probabilities multiply the values in 8 significant bits, as
- * bf16 has, as long as they are not tiny: of a value's tile of 128, the
- * smallest step is 2^-20 of the row's largest (probability times the key's
- * largest tile scale), times the tile's largest ratio of a key's scale to
- * that key's largest. So where one key alone has a tile whose scale is some
- * 2^14 or more above its other tiles' scales, few bits are left in those
- * other tiles. lse and the weights are formed from fp32 probabilities.
+ * others exactly. A probability times its key's tile scale is held to
+ * 1.4 * 2^-8 of itself at worst (bf16 has 2^-8; on average it is 2^-9.7), or,
+ * where that is more, to 2^-18 (mostly 2^-20) of the row's largest
+ * probability times largest tile scale of a key, times the largest ratio in
+ * the tile of any key's scale to that key's largest. So where one key alone
+ * has a tile whose scale is some 2^12 or more above its other tiles', few
+ * bits are left in those other tiles. lse and the weights are formed from
+ * fp32 probabilities.
  *
  * Arguments that the three calls share:
  *  q_latent      bf16 [num_tokens, num_heads, >= 512]; q_rope bf16
@@ -378,6 +379,8 @@ kvpub_status kvpub_epoch_wait(const unsigned long long *epoch,
  *                for every block of threads in which a wait ran into its
  *                limit (which no correct launch does). What such a block
  *                writes afterwards is NaN, with or without a counter.
+ *                Attention does not look at a sequence without query
+ *                tokens, and counts none of its blocks.
  *  lse           float [num_tokens, num_heads], contiguous.
  * Nothing else is read: rows of the cache past a sequence's length may hold
  * anything, also NaN codes, and a NaN or Inf in a row reaches only the query

@@ -66,8 +66,10 @@ namespace cg = cooperative_groups;
 
 // Probabilities are held times 2^kShift.  They may outgrow the reference
 // maximum by 2^kGrowth before it is moved (and the accumulators rescaled):
-// 2^(kShift + kGrowth) stays below E4M3's 448.  The smallest step of the two
-// 8-bit parts is then some 2^-20 of the row's largest probability.  (A move
+// 2^(kShift + kGrowth) stays below E4M3's 448.  Of the two 8-bit parts' sum 8 bits
+// are right down to 2^-12 of the row's largest probability; smaller ones are off by
+// up to 2^-20 of that, and by up to four times as much as powers of two stand for
+// the key's largest scale and for the tile's largest ratio.  (A move
 // costs a third of a unit; with 7 and 1.75 the attention took 2 % longer.)
 constexpr float kShift = 6.0f;
 constexpr float kGrowth = 2.75f;
